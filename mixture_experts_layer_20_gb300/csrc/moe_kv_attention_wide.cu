@@ -534,8 +534,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint4 v[8];
 #pragma unroll
           for (int u = 0; u < 8; ++u) v[u] = lds128(src + ((u ^ x) << 4));
-          __syncwarp();
-          if (lane == 0 && ok) mbar_arrive(empty + 8 * h.slot);
           if (n > 0) wait(o_done, (n - 1) & 1);
 #pragma unroll
           for (int u = 0; u < 16; ++u) {  // 8 columns each
@@ -544,6 +542,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             sts128(v_smem + (u >> 3) * (kTokens * 128) + tid * 128 + (((u & 7) ^ x) << 4),
                    codes_f16(lo), codes_f16_hi(lo), codes_f16(hi), codes_f16_hi(hi));
           }
+          // Only now is the slot given back: the loads are known to be done where their
+          // values have been used.  (Given back right after them, with the wait in
+          // between, some of the loads were done after it, when the slot was being
+          // filled again.)
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(empty + 8 * h.slot);
         }
         wait(s_done, n & 1);
         tc_fence_after_sync();
