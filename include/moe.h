@@ -417,8 +417,10 @@ moe_status_t moe_kv_append(const moe_kv_cache_t* cache, int layer, const moe_bf1
  * kv_lens).  out [T, heads, dim] bf16, lse [T, heads] fp32 (or NULL), scale
  * and head grouping as for moe_prompt_attention; a row that sees nothing gives
  * zeros and lse -infinity.  Scores, sums and the output are accumulated in
- * fp32; the weights enter the second product with 11 significant bits.  What
- * the pages hold past a sequence's length, and later tokens, take no part.
+ * fp32; the weights enter the second product with 11 significant bits (one
+ * below 2^-16 of its row's largest is off by up to 2^-27 of that), whatever the
+ * scales of other blocks; values of 2^-100 to 2^110 may stand beside each other.
+ * What the pages hold past a sequence's length, and later tokens, take no part.
  * The result does not depend on the other sequences' values or on timing; how
  * a sequence's keys are split (hence rounding) depends on the batch's sizes and
  * lengths and on max_pages.

@@ -36,8 +36,8 @@
 // row's bytes 32 t .. 32 t + 31 feeds them to the MMAs as they lie.  V comes
 // transposed by ldmatrix in pairs of bytes, which a byte permute splits into
 // even and odd columns (rows g and g + 8 of A), P by movmatrix.  The weights
-// p = 2^(s - m) enter as f16 p 2^6 2^(X - Xref), X the block's value scale and
-// Xref the largest so far: 11 significant bits, three more than bf16.  A row's
+// p = 2^(s - m) enter as f16 p 2^6 2^(X - ref), X the block's value scale and ref
+// the unit's (next_units): 11 significant bits, three more than bf16.  A row's
 // reference m is moved (a reduction over the warp, and O rescaled) only when
 // some score passes it by 2^8.
 
@@ -297,28 +297,351 @@ __device__ __forceinline__ void load_rings(const KvAttention& a, const CUtensorM
   }
 }
 
+// A unit's query rows as f16 fragments, each row over 2^e of its largest value, in
+// registers or at q_smem.  This lane loads row g of each tile; it keeps the scores'
+// factors of rows 2 t4 and 2 t4 + 1, its columns of S^T.  limit: the last position
+// that each row sees.
+template <class S>
+__device__ __forceinline__ void load_queries(const KvAttention& a, const Seq& q, int head, int r0,
+                                             int* limit, uint32_t q_smem,
+                                             uint32_t (&qf)[S::kQueryInSmem ? 1 : S::NT][S::D / 16][2],
+                                             float (&row_scale)[S::NT][2]) {
+  constexpr int D = S::D, NT = S::NT, kSteps = D / 16;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const int rows = q.fresh * a.group;  // of the sequence and head
+  uint4 raw[NT][D / 32];  // all loads under way before the first is used
+  int last[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = r0 + nt * 8 + g;
+    const bool valid = r < rows;
+    const int i = valid ? r / a.group : 0;
+    const int gh = valid ? r - i * a.group : 0;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (q.row0 + i) * a.q_stride +
+                               static_cast<size_t>(head * a.group + gh) * D + t4 * (D / 4);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+      raw[nt][c] = valid ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+    last[nt] = valid ? q.len - q.fresh + i : -1;
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float top = 0.0f;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      const uint32_t v[4] = {raw[nt][c].x, raw[nt][c].y, raw[nt][c].z, raw[nt][c].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[j] << 16)),
+                               fabsf(__uint_as_float(v[j] & 0xffff0000u))));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // exponent field e: values over 2^(e - 127) lie in [-2, 2]
+    const int e = min(253, max(1, static_cast<int>(__float_as_uint(top) >> 23)));
+    const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+    const float rs = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e) << 23);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      row_scale[nt][j] = __shfl_sync(0xffffffffu, rs, (2 * t4 + j) * 4);
+    if (t4 == 0) limit[nt * 8 + g] = last[nt];
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const uint32_t v0 = k & 1 ? raw[nt][k / 2].z : raw[nt][k / 2].x;
+      const uint32_t v1 = k & 1 ? raw[nt][k / 2].w : raw[nt][k / 2].y;
+      const uint32_t f0 =
+          pack_f16x2(__uint_as_float(v0 << 16) * down, __uint_as_float(v0 & 0xffff0000u) * down);
+      const uint32_t f1 =
+          pack_f16x2(__uint_as_float(v1 << 16) * down, __uint_as_float(v1 & 0xffff0000u) * down);
+      if constexpr (S::kQueryInSmem) {
+        sts64(q_smem + (nt * kSteps + k) * 256, f0, f1);
+      } else {
+        qf[nt][k][0] = f0;
+        qf[nt][k][1] = f1;
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// O / l in the values' own scale, from units of 2^(ref - 127 - kPBits): the result,
+// or a part of it.  nan_from: see clean_values; null where it noted nothing.
+template <class S>
+__device__ __forceinline__ void finish_unit(const KvAttention& a, const Seq& q, int head, int r0,
+                                            bool whole, float* part, const int* limit, int* nan_from,
+                                            int ref, float (&o)[S::D / 16][S::NT][4],
+                                            const float (&m)[S::NT][2], const float (&l)[S::NT][2]) {
+  constexpr int D = S::D, NT = S::NT, kChunks = D / 16;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const int rows = q.fresh * a.group;
+  if (nan_from) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (nan_from[16 * c + 2 * g + (j >> 1)] <= limit[nt * 8 + 2 * t4 + (j & 1)])
+            o[c][nt][j] = NAN;
+    __syncwarp();
+    for (int i = lane; i < D; i += 32) nan_from[i] = INT_MAX;
+  }
+  const float up = byte_scale(ref) * (1.0f / (1 << kPBits));
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float sum = l[nt][j];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      const int r = nt * 8 + 2 * t4 + j, row = r0 + r;
+      if (row >= rows) continue;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      if (whole) {
+        const int i = row / a.group;
+        const size_t orow =
+            static_cast<size_t>(q.row0 + i) * a.heads + head * a.group + (row - i * a.group);
+        uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + orow * D);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          out[8 * c + g] = pack_bf16x2(o[c][nt][j] * inv * up, o[c][nt][2 + j] * inv * up);
+        if (g == 0 && a.lse) a.lse[orow] = log_sum(m[nt][j], sum);
+      } else {
+        float2* dst = reinterpret_cast<float2*>(part + r * (D + 2));
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          dst[8 * c + g] = make_float2(o[c][nt][j] * inv * up, o[c][nt][2 + j] * inv * up);
+        if (g == 0) dst[D / 2] = make_float2(m[nt][j], sum);
+      }
+    }
+}
+
+// What a CTA's warps share.
+template <class S>
+struct Shared {
+  alignas(8) uint64_t bar[4 * S::kWarps * S::kStages];  // K full, V full, K empty, V empty
+  Rings<S> rings;
+  Walk<typename S::Deal> walk[S::kWarps];
+  int limit[S::kWarps][S::kRows];  // last position that a row sees
+  int nan[S::kWarps][S::D];        // see clean_values
+  int abort;
+};
+
+// Where a unit's part lies: the first in the second slot of its warp, the others in
+// the first of theirs.
+template <class S>
+__device__ __forceinline__ float* part_slot(const KvAttention& a, int warp, int t0) {
+  return a.partial + (static_cast<size_t>(blockIdx.x * S::kWarps + warp) * 2 + (t0 == 0 ? 1 : 0)) *
+                         S::kRows * (S::D + 2);
+}
+
+// The steps from t on of a warp's unit whose value scales lie far apart (K of the first
+// has landed), its steps before left as a part in its slot; the result, or a part of
+// it.  Block by block: a block's weights over its own largest as f16 p 2^6, and its
+// product (one MMA deep) added to O in fp32 with the block's factor, so that no
+// block's scale or weight takes bits from another's.  Out of line, and the state
+// handed over in memory: in line, or with O live across the call, the ordinary steps
+// of 16 rows took 2 to 30 % longer (registers).  64 sequences of up to 4096, 64 heads over
+// 4, half of the value blocks 2^12 above the others: 77 us for 55 (L2 flushed).
+// Stage and phase (in the high half) are the ring's, and returned; ~0: a wait gave up.
+template <class S, bool OWN>
+__device__ __noinline__ uint32_t far_steps(const KvAttention& a, Shared<S>& sh, uint32_t base, int t,
+                                           uint32_t at) {
+  constexpr int D = S::D, NT = S::NT, kSteps = D / 16, kChunks = D / 16;
+  constexpr int kN = S::kWarps * S::kStages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const WaitCtx wc{a.timeout_ns, a.status, &sh.abort};
+  const uint32_t ring = base + warp * S::kStages * S::kStage;
+  const uint32_t q_smem = base + kN * S::kStage + warp * S::kQuery + lane * 8;
+  const uint32_t k_full = smem_u32(&sh.bar[warp * S::kStages]);
+  const uint32_t v_full = k_full + 8 * kN, k_empty = k_full + 16 * kN, v_empty = k_full + 24 * kN;
+  const Walk<typename S::Deal>& w = sh.walk[warp];
+  const Seq q = w.q;
+  const int t1 = w.end(), r0 = w.group * S::kRows, rows = q.fresh * a.group;
+  const bool whole = w.step == 0 && t1 == w.steps;
+  int* const limit = sh.limit[warp];
+  int* const nan_from = sh.nan[warp];
+  // places of K's rows and V's matrices, as for the ordinary steps
+  const int x = D == 128 ? g : (g >> 1) & 3;
+  const int mi = lane >> 3, vr = lane & 7;
+  const int vx = (mi >> 1) ^ (D == 128 ? vr : (vr >> 1) & 3);
+  const uint32_t v_off = S::kHalf + static_cast<uint32_t>(((mi & 1) * 8 + vr) * D);
+  int stage = at & 0xffff;
+  uint32_t phase = at >> 16;
+  uint32_t qf[S::kQueryInSmem ? 1 : NT][kSteps][2];
+  float row_scale[NT][2];
+  load_queries<S>(a, q, w.head, r0, limit, q_smem, qf, row_scale);
+
+  // what the unit's earlier steps left
+  const float* const slot = part_slot<S>(a, warp, w.step);
+  constexpr float kDown = 1.0f / (1 << (kFarRef - 127 - kPBits));
+  float o[kChunks][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int r = nt * 8 + 2 * t4 + j;
+      const float2* src = reinterpret_cast<const float2*>(slot + r * (D + 2));
+      const bool there = r0 + r < rows;
+      const float2 ml = there ? src[D / 2] : make_float2(-INFINITY, 0.0f);
+      m[nt][j] = ml.x;
+      l[nt][j] = g == 0 ? ml.y : 0.0f;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        const float2 v = there ? src[8 * c + g] : make_float2(0.0f, 0.0f);
+        o[c][nt][j] = v.x * kDown * ml.y;
+        o[c][nt][2 + j] = v.y * kDown * ml.y;
+      }
+    }
+  bool ok = true, nans = false;
+#pragma unroll 1
+  for (; t < t1; ++t) {
+    const int pos = t * kStep;
+    const uint32_t sb = ring + stage * S::kStage;
+    const bool zone = pos + kStep - 1 > q.len - q.fresh;
+    ok = __all_sync(0xffffffffu, mbar_wait(k_full + 8 * stage, phase, wc));
+    if (!ok) break;
+    const uint4 words = sh.rings.scales[warp][stage];
+    const uint32_t shifts = sh.rings.shifts[warp][stage];
+    ok = __all_sync(0xffffffffu, mbar_wait(v_full + 8 * stage, phase, wc));
+    if (!ok) break;
+    if (zone && clean_values<D>(sb + S::kHalf, pos, q.len, q.fresh, nan_from)) nans = true;
+#pragma unroll 1
+    for (int b = 0; b < 2; ++b) {
+      const float ks =
+          byte_scale((b ? words.y >> (shifts >> 8 & 0xff) : words.x >> (shifts & 0xff)) & 0xff);
+      const float vs =
+          byte_scale((b ? words.w >> (shifts >> 24) : words.z >> (shifts >> 16 & 0xff)) & 0xff);
+      uint32_t kw[2][D / 16];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          const int chunk = D == 128 ? (2 * t4 + c) ^ x : t4 ^ x;
+          const uint4 v = lds128(sb + (b * 16 + h * 8 + g) * D + chunk * 16);
+          kw[h][4 * c] = v.x; kw[h][4 * c + 1] = v.y;
+          kw[h][4 * c + 2] = v.z; kw[h][4 * c + 3] = v.w;
+        }
+      float sc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[nt][j] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        const uint32_t ka[4] = {codes_f16(kw[0][k]), codes_f16(kw[1][k]), codes_f16_hi(kw[0][k]),
+                                codes_f16_hi(kw[1][k])};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if constexpr (S::kQueryInSmem) {
+            const uint2 qw = lds64(q_smem + (nt * kSteps + k) * 256);
+            mma_f16(sc[nt], ka, qw.x, qw.y);
+          } else {
+            mma_f16(sc[nt], ka, qf[nt][k][0], qf[nt][k][1]);
+          }
+        }
+      }
+      uint32_t pb[NT][2];
+      float gain[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float p[2][2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float f = ks * row_scale[nt][j];
+          float s[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            s[h] = sc[nt][2 * h + j] * f;
+            if (pos + 16 * b + g + 8 * h > limit[nt * 8 + 2 * t4 + j]) s[h] = -INFINITY;
+          }
+          float u = fmaxf(s[0], s[1]);
+          u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, 4));
+          u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, 8));
+          u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, 16));
+          const float fm = u > m[nt][j] ? ex2(m[nt][j] - u) : 1.0f;
+          m[nt][j] = fmaxf(m[nt][j], u);
+          l[nt][j] *= fm;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            o[c][nt][j] *= fm;
+            o[c][nt][2 + j] *= fm;
+          }
+          // a row that sees nothing of the block: weights and factor 0
+          const float top = u == -INFINITY ? 0.0f : u;
+          const float over = u == -INFINITY ? 0.0f : ex2(u - m[nt][j]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) p[h][j] = ex2(s[h] - top);
+          l[nt][j] += (p[0][j] + p[1][j]) * over;
+          gain[nt][j] = over * vs * pow2i(127 - kFarRef);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          pb[nt][h] = movmatrix(pack_f16x2(p[h][0] * (1 << kPBits), p[h][1] * (1 << kPBits)));
+      }
+#pragma unroll
+      for (int c = 0; c < kChunks; c += 2) {
+        uint32_t v[4];
+        ldmatrix_x4_trans(sb + v_off + b * 16 * D + ((vx ^ c) * 16), v);
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          const uint32_t a0 = __byte_perm(v[2 * cc], 0, 0x3120);
+          const uint32_t a1 = __byte_perm(v[2 * cc + 1], 0, 0x3120);
+          const uint32_t va[4] = {codes_f16(a0), codes_f16_hi(a0), codes_f16(a1), codes_f16_hi(a1)};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma_f16(d, va, pb[nt][0], pb[nt][1]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              o[c + cc][nt][j] = fmaf(d[j], gain[nt][j & 1], o[c + cc][nt][j]);
+          }
+        }
+      }
+    }
+    // clean_values wrote through the generic proxy what TMA writes next
+    if (zone) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();  // K, V and the scales are read
+    if (lane == 0) {
+      mbar_arrive(k_empty + 8 * stage);
+      mbar_arrive(v_empty + 8 * stage);
+    }
+    if (++stage == S::kStages) { stage = 0; phase ^= 1u; }
+  }
+  float* part = part_slot<S>(a, warp, w.step);
+  if constexpr (OWN) {
+    extern __shared__ uint8_t smem_raw[];
+    part = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)));
+  }
+  finish_unit<S>(a, q, w.head, r0, whole, part, limit, nans ? nan_from : nullptr, kFarRef, o, m, l);
+  return ok ? static_cast<uint32_t>(stage) | phase << 16 : ~0u;
+}
+
 // OWN: each CTA has a unit of its own and shares its steps out among its warps,
 // which leave their parts in shared memory, where the CTA joins them: for few
 // units of few steps, where the second kernel would cost more than the even
 // dealing gains.
 template <class S, bool OWN>
 __global__ void __launch_bounds__(S::kThreads, 1)
-    moe_kv_attention_kernel(const __grid_constant__ CUtensorMap map, const KvAttention a) {
+    moe_kv_attention_kernel(const __grid_constant__ CUtensorMap map,
+                            const __grid_constant__ KvAttention a) {
   constexpr int D = S::D, NT = S::NT;
   using Deal = typename S::Deal;
   constexpr int kSteps = D / 16;   // MMA steps of a score
   constexpr int kChunks = D / 16;  // 16-byte chunks of a row
   constexpr int kN = S::kWarps * S::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ alignas(8) uint64_t s_bar[4 * kN];  // K full, V full, K empty, V empty
-  __shared__ Rings<S> s_rings;
+  __shared__ Shared<S> sh;
   __shared__ Seq s_seqs[kSeqCache];
-  __shared__ Walk<typename S::Deal> s_walk[S::kWarps];
-  __shared__ int s_limit[S::kWarps][S::kRows];  // last position that a row sees
-  __shared__ int s_nan[S::kWarps][D];           // see clean_values
   __shared__ long long s_sum[S::kThreads / 32];
   __shared__ bool s_any[S::kWarps];
-  __shared__ int s_abort;
+  uint64_t* const s_bar = sh.bar;
+  auto& s_rings = sh.rings;
+  auto& s_walk = sh.walk;
+  auto& s_limit = sh.limit;
+  auto& s_nan = sh.nan;
+  int& s_abort = sh.abort;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -408,70 +731,12 @@ __global__ void __launch_bounds__(S::kThreads, 1)
 
   for (bool go = !OWN || s_any[warp]; go;) {
     const int len = w.q.len, fresh = w.q.fresh;
-    const int rows = fresh * a.group;  // of the sequence and head
     const int r0 = w.group * S::kRows;
     const int t0 = w.step, t1 = w.end();
 
-    // Query rows as f16 fragments, each row over 2^e of its largest value.
-    // This lane loads row g of each tile; it keeps the scores' factors of rows
-    // 2 t4 and 2 t4 + 1, its columns of S^T.
     uint32_t qf[S::kQueryInSmem ? 1 : NT][kSteps][2];
     float row_scale[NT][2];
-    uint4 raw[NT][D / 32];  // all loads under way before the first is used
-    int last[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = r0 + nt * 8 + g;
-      const bool valid = r < rows;
-      const int i = valid ? r / a.group : 0;
-      const int gh = valid ? r - i * a.group : 0;
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
-                                 (w.q.row0 + i) * a.q_stride +
-                                 static_cast<size_t>(w.head * a.group + gh) * D + t4 * (D / 4);
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c)
-        raw[nt][c] =
-            valid ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
-      last[nt] = valid ? len - fresh + i : -1;
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float top = 0.0f;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        const uint32_t v[4] = {raw[nt][c].x, raw[nt][c].y, raw[nt][c].z, raw[nt][c].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[j] << 16)),
-                                 fabsf(__uint_as_float(v[j] & 0xffff0000u))));
-      }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // exponent field e: values over 2^(e - 127) lie in [-2, 2]
-      const int e = min(253, max(1, static_cast<int>(__float_as_uint(top) >> 23)));
-      const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-      const float rs = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(e) << 23);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        row_scale[nt][j] = __shfl_sync(0xffffffffu, rs, (2 * t4 + j) * 4);
-      if (t4 == 0) s_limit[warp][nt * 8 + g] = last[nt];
-#pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        const uint32_t v0 = k & 1 ? raw[nt][k / 2].z : raw[nt][k / 2].x;
-        const uint32_t v1 = k & 1 ? raw[nt][k / 2].w : raw[nt][k / 2].y;
-        const uint32_t f0 = pack_f16x2(__uint_as_float(v0 << 16) * down,
-                                       __uint_as_float(v0 & 0xffff0000u) * down);
-        const uint32_t f1 = pack_f16x2(__uint_as_float(v1 << 16) * down,
-                                       __uint_as_float(v1 & 0xffff0000u) * down);
-        if constexpr (S::kQueryInSmem) {
-          sts64(q_smem + (nt * kSteps + k) * 256, f0, f1);
-        } else {
-          qf[nt][k][0] = f0;
-          qf[nt][k][1] = f1;
-        }
-      }
-    }
-    __syncwarp();
+    load_queries<S>(a, w.q, w.head, r0, s_limit[warp], q_smem, qf, row_scale);
 
     float o[kChunks][NT][4];  // columns 16 c + 2 g, + 1 (rows g, g + 8 of A) of rows 2 t4, + 1
     float m[NT][2], l[NT][2];
@@ -484,10 +749,11 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       m[nt][0] = m[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.0f;
     }
-    int ref = 0;  // largest value-scale byte so far
+    int ref = 0;  // O's units, see next_units
     bool nans = false;
 
-    for (int t = t0; t < t1 && ok && len > 0; ++t) {
+    int t = t0;
+    for (; t < t1 && ok && len > 0; ++t) {
       const int pos = t * kStep;  // first token of the step
       const uint32_t sb = ring + stage * S::kStage;
       ok = __all_sync(0xffffffffu, mbar_wait(k_full + 8 * stage, phase, wc));
@@ -503,6 +769,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         vbyte[0] = words.z >> (shifts >> 16 & 0xff) & 0xff;
         vbyte[1] = words.w >> (shifts >> 24) & 0xff;
       }
+      // byte 0, as where there is no block, is left out of account
+      const int next = next_units(ref, min(vbyte[0] ? vbyte[0] : 255, vbyte[1] ? vbyte[1] : 255),
+                                  max(vbyte[0], vbyte[1]));
+      if (next < 0) break;  // far_steps does the rest
       {
         float sc[2][NT][4];
 #pragma unroll
@@ -562,8 +832,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
                   sc[b][nt][j] = -INFINITY;
               }
         }
-        const int new_ref = max(ref, max(vbyte[0], vbyte[1]));
-        bool grow = new_ref != ref;
+        bool grow = next != ref;
         float top[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -574,8 +843,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             grow = grow || top[nt][j] > m[nt][j] + kGrow;
           }
         if (__any_sync(0xffffffffu, grow)) {
-          const float fr = pow2i(ref - new_ref);
-          ref = new_ref;
+          const float fr = pow2i(ref - next);
+          ref = next;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -641,55 +910,18 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       if (++stage == S::kStages) { stage = 0; phase ^= 1u; }
     }
 
-    if (nans) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (s_nan[warp][16 * c + 2 * g + (j >> 1)] <= s_limit[warp][nt * 8 + 2 * t4 + (j & 1)])
-              o[c][nt][j] = NAN;
-      __syncwarp();
-      for (int i = lane; i < D; i += 32) s_nan[warp][i] = INT_MAX;
-    }
-
-    // ---- O / l in the values' own scale: the result, or a part of it
+    // (OWN: a part lies in the warp's ring, whose loads are all read.)
+    const bool far = ok && t < t1 && len > 0;
     const bool whole = t0 == 0 && t1 == w.steps;
-    // The unit's first part lies in the second slot of its warp, the others in
-    // the first of theirs.
-    // (OWN: in the warp's ring, whose loads are all read.)
-    float* const part = OWN ? own_part(warp) : a.partial + (static_cast<size_t>(gw) * 2 + (t0 == 0 ? 1 : 0)) * S::kRows *
-                                        (D + 2);
-    const float up = byte_scale(ref) * (1.0f / (1 << kPBits));
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float sum = l[nt][j];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        const int r = nt * 8 + 2 * t4 + j, row = r0 + r;
-        if (row >= rows) continue;
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        if (whole) {
-          const int i = row / a.group;
-          const size_t orow =
-              static_cast<size_t>(w.q.row0 + i) * a.heads + w.head * a.group + (row - i * a.group);
-          uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + orow * D);
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            out[8 * c + g] = pack_bf16x2(o[c][nt][j] * inv * up, o[c][nt][2 + j] * inv * up);
-          if (g == 0 && a.lse) a.lse[orow] = log_sum(m[nt][j], sum);
-        } else {
-          float2* dst = reinterpret_cast<float2*>(part + r * (D + 2));
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            dst[8 * c + g] = make_float2(o[c][nt][j] * inv * up, o[c][nt][2 + j] * inv * up);
-          if (g == 0) dst[D / 2] = make_float2(m[nt][j], sum);
-        }
-      }
+    finish_unit<S>(a, w.q, w.head, r0, whole && !far,
+                   OWN && !far ? own_part(warp) : part_slot<S>(a, warp, t0), s_limit[warp],
+                   nans ? s_nan[warp] : nullptr, ref, o, m, l);
+    if (far) {
+      const uint32_t at = far_steps<S, OWN>(a, sh, base, t, stage | phase << 16);
+      ok = at != ~0u;
+      stage = at & 0xffff;
+      phase = at >> 16;
+    }
     // After a wait that gave up the other units are walked too: what is not
     // computed is written as it stands.
     __syncwarp();

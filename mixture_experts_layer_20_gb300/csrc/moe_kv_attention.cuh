@@ -63,6 +63,33 @@ __device__ __forceinline__ float pow2i(int k) {
   return k < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(min(k, 127) + 127) << 23);
 }
 
+// What O is in units of while a unit's blocks of values, each with a scale of its
+// own, go by.  A weight enters the second product as f16 p 2^6 2^(X - ref), X the
+// scale byte of its value block, O in units of 2^(ref - 127 - 6).  f16 has its 11
+// bits down to 2^-14 and nothing below 2^-25, so X may lie at most kNear under
+// ref: a weight of 2^-16 of its row's largest then still has all of them, and
+// what is lost at the low end is 2^-27 of the largest.  ref follows the blocks up
+// and down, from kLeast to kMost (block maxima of 2^-55 to 2^25; O is moved with it,
+// exactly in fp32).  A step of blocks further apart, or beyond these, makes the unit
+// `far` for the rest of its steps here: each block is then added to O by itself, in
+// fp32, and O is in units of 2^(kFarRef - 127 - 6).  That holds values of 2^-100 to
+// 2^110 beside each other, whatever their blocks' scales and weights.
+// Blocks with byte 0 (no value above 2^-118; zeros, as a rule) are left out of
+// account.
+constexpr int kNear = 4, kLeast = 64, kMost = 144, kFarRef = 151;
+// Whether ref serves for a step whose blocks' bytes lie in lo .. hi (255 .. 0: none).
+__device__ __forceinline__ bool units_hold(int ref, int lo, int hi) {
+  return hi <= ref && lo >= ref - kNear;
+}
+// The ref that does (ref: the last one, 0 before any values), -1: none, it is far.
+__device__ __forceinline__ int next_units(int ref, int lo, int hi) {
+  const int top = max(ref, hi);
+  const int next = lo < top - kNear ? hi : top;
+  const bool near = lo >= next - kNear &&
+                    (next == 0 || static_cast<unsigned>(next - kLeast) <= kMost - kLeast);
+  return near ? next : -1;
+}
+
 // One sequence, with indexes that do not fit turned into nothing to do.
 struct Seq {
   int row0, fresh, len;  // rows of q and their number, keys

@@ -14,8 +14,10 @@
 //     stay in the threads until the unit's end, and a row's reference m moves
 //     only when some score passes it by 2^8 (one vote a step);
 //   O^T [column, row] += V^T P^T: V as f16 in shared memory, read M-major, so
-//     that the transposition costs nothing; P as f16 2^6 2^(X - Xref), X the
-//     block's value scale and Xref the largest so far.
+//     that the transposition costs nothing; P as f16 2^6 2^(X - ref), X the
+//     block's value scale and ref the unit's (next_units).
+// Where value scales lie far apart, O's part of a step is added up in fp32
+// instead (far_steps): no block's scale takes bits from another's weights.
 // Two groups an SM, each with its own share of the steps, its own loading warp
 // and a ring of 64-token halves of K and V; the loading warp looks pages up
 // two steps and scales one step ahead.
@@ -41,8 +43,8 @@ constexpr int kSlots = 7;         // of 64 tokens' codes, K or V, in a group's r
 constexpr int kScaleSlots = 4;    // steps whose scales are kept
 constexpr int kThreads = (kGroups + 1) * 128;  // the last warpgroup: a loading and an MMA warp a group
 constexpr int kBars = 2 * kSlots + 4;
-constexpr uint32_t kGroupCols = 128;           // tensor memory: K, S, O
-constexpr uint32_t kColS = 64, kColO = 96;
+constexpr uint32_t kGroupCols = 256;           // tensor memory: K, S, O; a far unit's O, sums
+constexpr uint32_t kColS = 64, kColO = 96, kColFar = 128, kColFarSum = 160;
 
 using Deal = DealOf<ROWS, kTokens, 1>;
 constexpr int kVBytes = kTokens * D * 2;     // V as f16
@@ -116,8 +118,9 @@ struct Half {
 };
 
 __device__ __forceinline__ void load_group(const KvAttention& a, const CUtensorMap* map, Walk<Deal> w,
-                                           const Seq* cache, uint8_t (*scales)[16], uint32_t ring,
-                                           uint32_t full, uint32_t empty, const WaitCtx& wc) {
+                                           const Seq* cache, uint8_t (*scales)[16], uint32_t* range,
+                                           uint32_t ring, uint32_t full, uint32_t empty,
+                                           const WaitCtx& wc) {
   const int lane = threadIdx.x & 31;
   const int P = a.cache.page, ps = __ffs(P) - 1, box = min(P, 32);  // P is a power of two
   const int block = lane & 7;  // of the step, that this lane is for
@@ -188,8 +191,13 @@ __device__ __forceinline__ void load_group(const KvAttention& a, const CUtensorM
                     (((s0.page * 2 + (part >> 1)) * a.cache.heads + s0.head) << ps) +
                         (s0.at & (P - 1)));
       // the scales may still be on their way: they go with the first arrival
-      if (part == 0 && lane < 16)
-        scales[step % kScaleSlots][lane] = static_cast<uint8_t>(s0.scale);
+      if (part == 0) {
+        const unsigned v = lane >= 8 && lane < 16 ? s0.scale : 0;  // the values'
+        const unsigned hi = __reduce_max_sync(0xffffffffu, v);
+        const unsigned lo = __reduce_min_sync(0xffffffffu, v ? v : 255u);
+        if (lane < 16) scales[step % kScaleSlots][lane] = static_cast<uint8_t>(s0.scale);
+        if (lane == 0) range[step % kScaleSlots] = lo | hi << 8;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(full + 8 * h.slot, boxes * box * D);
       ++n;
@@ -284,30 +292,308 @@ __device__ __forceinline__ void issue_group(const KvAttention& a, Walk<Deal> w, 
   }
 }
 
+// One thread of a group: its group's places, and its own.
+struct GroupAt {
+  uint32_t ring, full, empty, s_done, o_done, ready;
+  uint32_t v_smem, q_smem, p_smem;
+  uint32_t mine;  // tensor memory, at this warp's lanes
+  int group, tid, half;  // tid: token of a step, column of O; half: of the step's tokens
+};
+
+// The K half of step i (of this group's, in turn) into tensor memory.  Here and
+// below: whether no wait has given up, in the warp, so far.  After one that has no
+// slot of the ring is given back: its load may still be under way, and another
+// arrival in that phase of its barrier would be one too many.
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t phase, const WaitCtx& wc, bool ok) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, phase, wc)) && ok;
+}
+__device__ __forceinline__ bool take_k(const GroupAt& g, uint32_t i, const WaitCtx& wc, bool ok) {
+  const Half h(4 * i + g.half);
+  ok = wait_all(g.full + 8 * h.slot, h.phase, wc, ok);
+  const uint32_t src = g.ring + h.slot * kHalfBytes + static_cast<uint32_t>(g.tid & 63) * D;
+  const int x = g.tid & 7;  // swizzle of this token's rows
+  uint4 k[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) k[u] = lds128(src + ((u ^ x) << 4));
+#pragma unroll
+  for (int hh = 0; hh < 2; ++hh) {
+    uint32_t f[32];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t v[4] = {k[4 * hh + u].x, k[4 * hh + u].y, k[4 * hh + u].z, k[4 * hh + u].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[8 * u + 2 * j] = codes_f16(v[j]);
+        f[8 * u + 2 * j + 1] = codes_f16_hi(v[j]);
+      }
+    }
+    tmem_st_x32(g.mine + 32 * hh, f);
+  }
+  __syncwarp();
+  if ((g.tid & 31) == 0 && ok) mbar_arrive(g.empty + 8 * h.slot);
+  return ok;
+}
+// V of step n as f16, over the last one (whose product is complete).
+__device__ __forceinline__ bool take_v(const GroupAt& g, uint32_t n, bool zone, int at, int len,
+                                       int fresh, int* nan_from, int* nans, const WaitCtx& wc,
+                                       bool ok) {
+  const Half h(4 * n + 2 + g.half);
+  ok = wait_all(g.full + 8 * h.slot, h.phase, wc, ok);
+  const uint32_t src = g.ring + h.slot * kHalfBytes + static_cast<uint32_t>(g.tid & 63) * D;
+  const int x = g.tid & 7;
+  if (zone) clean_row(src, x, at, len, fresh, nan_from, nans);
+  uint4 v[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) v[u] = lds128(src + ((u ^ x) << 4));
+  if (n > 0) ok = wait_all(g.o_done, (n - 1) & 1, wc, ok);
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {  // 8 columns each
+    const uint32_t lo = u & 1 ? v[u >> 1].z : v[u >> 1].x;
+    const uint32_t hi = u & 1 ? v[u >> 1].w : v[u >> 1].y;
+    sts128(g.v_smem + (u >> 3) * (kTokens * 128) + g.tid * 128 + (((u & 7) ^ x) << 4),
+           codes_f16(lo), codes_f16_hi(lo), codes_f16(hi), codes_f16_hi(hi));
+  }
+  // Only now is the slot given back: the loads are known to be done where their values
+  // have been used.  (Given back right after them, with the wait in between, some of
+  // the loads were done after it, when the slot was being filled again.)
+  __syncwarp();
+  if ((g.tid & 31) == 0 && ok) mbar_arrive(g.empty + 8 * h.slot);
+  return ok;
+}
+// This warp's operands are written: to the MMA warp.
+__device__ __forceinline__ void hand_over(const GroupAt& g) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  tmem_st_wait();
+  tc_fence_before_sync();
+  __syncwarp();
+  if ((g.tid & 31) == 0) mbar_arrive(g.ready);
+}
+
+// What a CTA's threads share.
+struct Shared {
+  alignas(8) uint64_t bar[kGroups * kBars];
+  Walk<Deal> walk[kGroups];
+  alignas(16) float scale[kGroups][ROWS];   // of a row's scores, from its f16
+  alignas(16) int limit[kGroups][ROWS];     // last position that a row sees
+  alignas(16) float m[kGroups][ROWS];       // its reference
+  alignas(16) float f[kGroups][ROWS];       // factors for all threads
+  float red[kGroups][4][ROWS];
+  alignas(16) uint8_t bytes[kGroups][kScaleSlots][16];
+  uint32_t range[kGroups][kScaleSlots];     // the values' bytes: smallest (but 0), largest
+  int nan[kGroups][D];  // first position of a NaN among the new tokens' values
+  int nans[kGroups];
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ GroupAt group_at(Shared& sh, uint32_t base, int group) {
+  const uint32_t ring = base + group * kGroupBytes, full = smem_u32(&sh.bar[group * kBars]);
+  const int tid = threadIdx.x & 127;
+  GroupAt g;
+  g.ring = ring;
+  g.v_smem = ring + kSlots * kHalfBytes;
+  g.q_smem = g.v_smem + kVBytes;
+  g.p_smem = g.q_smem + kQBytes;
+  g.full = full;
+  g.empty = full + 8 * kSlots;
+  g.s_done = full + 16 * kSlots;
+  g.o_done = g.s_done + 8;
+  g.ready = g.s_done + 16;
+  g.mine = sh.tmem_base + group * kGroupCols + (static_cast<uint32_t>(tid & 96) << 16);
+  g.group = group;
+  g.tid = tid;
+  g.half = tid >> 6;
+  return g;
+}
+
+// The steps from t on of a group's unit whose value scales lie far apart (n: steps of
+// this group so far), the first with its V in place and its scores at kColS: O += V P
+// in fp32, 8 rows a warp, 4 columns a lane, so that no block's scale takes bits from
+// another's weights.  O comes from kColO in units of 2^(was - 127 - kPBits) and goes to
+// kColFar in units of 2^(kFarRef - 127 - kPBits), the sums are at kColFarSum; the MMA
+// warp goes on as ever, what it adds up is not used.  32 sequences of up to 6000 with 4
+// new tokens, 64 heads over 8, half of the value blocks 2^12 above the others: 381 us for
+// 85 (L2 flushed).  Out of line: in line it cost a change of unit 2 us where the code
+// is cold.
+// Returns n after it, with the top bit where a wait gave up.
+__device__ __noinline__ uint32_t far_steps(const KvAttention& a, Shared& sh, uint32_t base, int t,
+                                           uint32_t n, int was) {
+  const int group = threadIdx.x >> 7;
+  const GroupAt g = group_at(sh, base, group);
+  const WaitCtx wc{a.timeout_ns, a.status, &sh.abort};
+  const Walk<Deal>& w = sh.walk[group];
+  const int len = w.q.len, fresh = w.q.fresh, t1 = w.end();
+  const int lane = g.tid & 31, quarter = g.tid >> 5, x = g.tid & 7;
+  bool ok = true;
+  uint64_t o[4][4];  // column 4 lane + c of rows 8 quarter + 2 j, + 1
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[c][j] = 0;
+  if (t != w.step) {  // in the new units, in two factors (each a normal number)
+    const int down = was - kFarRef;
+    const float f0 = pow2i(down / 2), f1 = pow2i(down - down / 2);
+    uint32_t r[ROWS];
+    tmem_ld_x32(g.mine + kColO, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // from a column a thread, 16 rows at a time
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        sts32(g.p_smem + (j * D + g.tid) * 4,
+              __float_as_uint(__uint_as_float(r[16 * h + j]) * f0 * f1));
+      group_sync(group);
+      if ((quarter >> 1) == h) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t at = g.p_smem + ((8 * (quarter & 1) + 2 * j) * D + 4 * lane) * 4;
+          const uint4 x0 = lds128(at), x1 = lds128(at + D * 4);
+          o[0][j] = pair(__uint_as_float(x0.x), __uint_as_float(x1.x));
+          o[1][j] = pair(__uint_as_float(x0.y), __uint_as_float(x1.y));
+          o[2][j] = pair(__uint_as_float(x0.z), __uint_as_float(x1.z));
+          o[3][j] = pair(__uint_as_float(x0.w), __uint_as_float(x1.w));
+        }
+      }
+      group_sync(group);
+    }
+  }
+  for (bool entry = true; t < t1; ++t, ++n, entry = false) {
+    const int at = t * kTokens + g.tid;
+    const bool zone = t * kTokens + kTokens - 1 > len - fresh;
+    if (!entry) {
+      ok = take_v(g, n, zone, at, len, fresh, sh.nan[group], &sh.nans[group], wc, ok);
+      ok = wait_all(g.s_done, n & 1, wc, ok);
+      tc_fence_after_sync();
+    }
+    uint32_t s[ROWS];
+    tmem_ld_x32(g.mine + kColS, s);
+    const uint8_t* const bytes = sh.bytes[group][n % kScaleSlots];
+    const float ks = byte_scale(bytes[g.tid / kKvBlock]);
+    tmem_ld_wait();
+    if (!entry && t + 1 < t1) ok = take_k(g, n + 1, wc, ok);
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      const float y = __uint_as_float(s[j]) * (sh.scale[group][j] * ks);
+      s[j] = at > sh.limit[group][j] ? 0xff800000u : __float_as_uint(y);
+      const int top = __reduce_max_sync(0xffffffffu, ordered(__uint_as_float(s[j])));
+      if (lane == j) sh.red[group][quarter][j] = unordered(top);
+    }
+    group_sync(group);
+    if (g.tid < ROWS) {
+      const float old = sh.m[group][g.tid];
+      const float u = fmaxf(fmaxf(sh.red[group][0][g.tid], sh.red[group][1][g.tid]),
+                            fmaxf(sh.red[group][2][g.tid], sh.red[group][3][g.tid]));
+      sh.f[group][g.tid] = u > old ? ex2(old - u) : 1.0f;
+      sh.m[group][g.tid] = fmaxf(old, u);
+    }
+    group_sync(group);
+    {
+      uint32_t l[ROWS];
+      tmem_ld_x32(g.mine + kColFarSum, l);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        const float m = sh.m[group][j];
+        const float p = ex2(__uint_as_float(s[j]) - (m == -INFINITY ? 0.0f : m));
+        s[j] = __float_as_uint(p);
+        l[j] = __float_as_uint(fmaf(__uint_as_float(l[j]), sh.f[group][j], p));
+      }
+      tmem_st_x32(g.mine + kColFarSum, l);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = *reinterpret_cast<const float2*>(&sh.f[group][8 * quarter + 2 * j]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[c][j] = mul2(o[c][j], pair(f.x, f.y));
+    }
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {  // 64 tokens' weights at a time, where P has its place
+      // a token's weights: 128 bytes, their 16-byte units turned by the token
+      if ((g.tid >> 6) == i) {
+#pragma unroll
+        for (int u = 0; u < ROWS / 4; ++u)
+          sts128(g.p_smem + (g.tid & 63) * (ROWS * 4) + ((u ^ x) << 4), s[4 * u], s[4 * u + 1],
+                 s[4 * u + 2], s[4 * u + 3]);
+      }
+      group_sync(group);
+      const uint32_t v = g.v_smem + (lane >> 4) * (kTokens * 128) + i * (64 * 128) + (lane & 1) * 8;
+      const int unit = lane >> 1 & 7;  // of the columns, in a token's 128 bytes
+#pragma unroll 1
+      for (int b = 0; b < 64 / kKvBlock; ++b) {
+        const float scale = byte_scale(bytes[8 + 4 * i + b]) * pow2i(127 - kFarRef + kPBits);
+#pragma unroll 4
+        for (int k = 0; k < kKvBlock; ++k) {
+          const int token = b * kKvBlock + k;
+          uint32_t h[2];
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                       : "=r"(h[0]), "=r"(h[1])
+                       : "r"(v + token * 128 + ((unit ^ (k & 7)) << 4))
+                       : "memory");
+          const uint32_t row = g.p_smem + token * (ROWS * 4);
+          const uint4 p0 = lds128(row + (((2 * quarter) ^ (k & 7)) << 4));
+          const uint4 p1 = lds128(row + (((2 * quarter + 1) ^ (k & 7)) << 4));
+          const uint64_t p[4] = {pair(__uint_as_float(p0.x), __uint_as_float(p0.y)),
+                                 pair(__uint_as_float(p0.z), __uint_as_float(p0.w)),
+                                 pair(__uint_as_float(p1.x), __uint_as_float(p1.y)),
+                                 pair(__uint_as_float(p1.z), __uint_as_float(p1.w))};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[c >> 1]));
+            const float value = (c & 1 ? f.y : f.x) * scale;
+            const uint64_t v2 = pair(value, value);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[c][j] = fma2(p[j], v2, o[c][j]);
+          }
+        }
+      }
+      group_sync(group);
+    }
+    if (t + 1 == t1) {  // to a column a thread, through V's memory
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 y[4] = {unpair(o[0][j]), unpair(o[1][j]), unpair(o[2][j]), unpair(o[3][j])};
+        const uint32_t at = g.v_smem + ((8 * quarter + 2 * j) * D + 4 * lane) * 4;
+        sts128(at, __float_as_uint(y[0].x), __float_as_uint(y[1].x), __float_as_uint(y[2].x),
+               __float_as_uint(y[3].x));
+        sts128(at + D * 4, __float_as_uint(y[0].y), __float_as_uint(y[1].y),
+               __float_as_uint(y[2].y), __float_as_uint(y[3].y));
+      }
+      group_sync(group);
+      uint32_t r[ROWS];
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) r[j] = lds32(g.v_smem + (j * D + g.tid) * 4);
+      tmem_st_x32(g.mine + kColFar, r);
+    }
+    hand_over(g);
+  }
+  return n | (ok ? 0u : 0x80000000u);
+}
+
 // After a wait that gave up, every wait returns at once: the groups' warps then
 // run their loops to the end with what there is, so that all of a group meet at
 // its barriers; the loading warps stop.
 __global__ void __launch_bounds__(kThreads, 1)
-    moe_kv_attention_wide_kernel(const __grid_constant__ CUtensorMap map, const KvAttention a) {
+    moe_kv_attention_wide_kernel(const __grid_constant__ CUtensorMap map,
+                                 const __grid_constant__ KvAttention a) {
   constexpr int kPerRow = kTokens / ROWS;  // threads that share a query row's load
   constexpr int kCols = D / kPerRow;       // its values that each takes
   extern __shared__ uint8_t smem_raw[];
-  __shared__ alignas(8) uint64_t s_bar[kGroups * kBars];
+  __shared__ Shared sh;
   __shared__ Seq s_seqs[kSeqCache];
-  __shared__ Walk<Deal> s_walk[kGroups];
-  __shared__ alignas(16) float s_scale[kGroups][ROWS];   // of a row's scores, from its f16
-  __shared__ alignas(16) int s_limit[kGroups][ROWS];     // last position that a row sees
-  __shared__ alignas(16) float s_m[kGroups][ROWS];       // its reference
-  __shared__ alignas(16) float s_f[kGroups][ROWS];       // factors for all threads
-  __shared__ float s_red[kGroups][4][ROWS];
   __shared__ int s_to[kGroups][ROWS];                    // a row's place among the results, or -1
-  __shared__ alignas(16) uint8_t s_bytes[kGroups][kScaleSlots][16];
-  __shared__ int s_nan[kGroups][D];  // first position of a NaN among the new tokens' values
-  __shared__ int s_nans[kGroups];
   __shared__ long long s_sum[kThreads / 32];
   __shared__ bool s_any[kGroups], s_more[kGroups];
-  __shared__ uint32_t s_tmem_base;
-  __shared__ int s_abort;
+  auto& s_bar = sh.bar;
+  auto& s_walk = sh.walk;
+  auto& s_scale = sh.scale;
+  auto& s_limit = sh.limit;
+  auto& s_m = sh.m;
+  auto& s_f = sh.f;
+  auto& s_red = sh.red;
+  auto& s_bytes = sh.bytes;
+  auto& s_range = sh.range;
+  auto& s_nan = sh.nan;
+  auto& s_nans = sh.nans;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
@@ -334,12 +620,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(b + 16 * kSlots + 16, 4);
       mbar_init(b + 16 * kSlots + 24, 1);
     }
-    s_abort = 0;
+    sh.abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&map);
   }
   pdl_wait_and_release();
-  const WaitCtx wc{a.timeout_ns, a.status, &s_abort};
+  const WaitCtx wc{a.timeout_ns, a.status, &sh.abort};
 
   // All steps, then this group's share of them.
   long long total = 0;
@@ -359,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (per * (static_cast<long long>(blockIdx.x) * kGroups) >= total) return;  // the whole CTA
   const int worker = blockIdx.x * kGroups + group;
   if (warp == 0) {
-    tmem_alloc(smem_u32(&s_tmem_base), kGroups * kGroupCols);
+    tmem_alloc(smem_u32(&sh.tmem_base), kGroups * kGroupCols);
     tmem_relinquish();
   }
   if (loads && !issues) {
@@ -379,9 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (any) share = s_walk[group];
     __syncthreads();  // the loading warps have their copies of the walks
     if (any && !issues)
-      load_group(a, &map, share, s_seqs, s_bytes[group], ring, full, empty, wc);
+      load_group(a, &map, share, s_seqs, s_bytes[group], s_range[group], ring, full, empty, wc);
     if (any && issues) {
-      const uint32_t tm = __shfl_sync(0xffffffffu, s_tmem_base, 0) + group * kGroupCols;
+      const uint32_t tm = __shfl_sync(0xffffffffu, sh.tmem_base, 0) + group * kGroupCols;
       issue_group(a, share, s_seqs, tm, q_smem, p_smem, v_smem, s_done, o_done, ready, wc);
       // Every MMA issued completes before tensor memory is freed.
       const bool leader = elect_one();
@@ -394,22 +680,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     const int tid = threadIdx.x & 127;  // token of a step, column of O
     const int quarter = warp & 3, half = quarter >> 1;
-    const uint32_t tm = __shfl_sync(0xffffffffu, s_tmem_base, 0) + group * kGroupCols;
+    const uint32_t tm = __shfl_sync(0xffffffffu, sh.tmem_base, 0) + group * kGroupCols;
     const uint32_t mine = tm + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t row_off = static_cast<uint32_t>(tid & 63) * D;
-    const int x = tid & 7;  // swizzle of this token's rows
+    const GroupAt g{ring, full, empty, s_done, o_done, ready, v_smem, q_smem, p_smem, mine, group, tid,
+                    half};
     uint32_t n = 0;         // steps so far
     const Walk<Deal>& w = s_walk[group];
     s_nan[group][tid] = INT_MAX;
     if (tid == 0) s_nans[group] = 0;
 
-    // The warp together again.  After a wait that gave up no slot of the ring is
-    // given back: its load may still be under way, and another arrival in that
-    // phase of its barrier would be one too many.
-    bool ok = true;
-    auto wait = [&](uint32_t bar, uint32_t phase) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar, phase, wc)) && ok;
-    };
+    bool ok = true;  // see take_k
+    auto wait = [&](uint32_t bar, uint32_t phase) { ok = wait_all(bar, phase, wc, ok); };
 
     // A unit, and this thread's part of its query rows.
     struct Unit {
@@ -433,41 +714,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     Unit unit{};
     if (any) unit = read_unit();
-
-    // The K half of step i (of this group's, in turn) into tensor memory.
-    auto take_k = [&](uint32_t i) {
-      const Half h(4 * i + half);
-      wait(full + 8 * h.slot, h.phase);
-      const uint32_t src = ring + h.slot * kHalfBytes + row_off;
-      uint4 k[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) k[u] = lds128(src + ((u ^ x) << 4));
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        uint32_t f[32];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint32_t v[4] = {k[4 * hh + u].x, k[4 * hh + u].y, k[4 * hh + u].z,
-                                 k[4 * hh + u].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            f[8 * u + 2 * j] = codes_f16(v[j]);
-            f[8 * u + 2 * j + 1] = codes_f16_hi(v[j]);
-          }
-        }
-        tmem_st_x32(mine + 32 * hh, f);
-      }
-      __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(empty + 8 * h.slot);
-    };
-    // This warp's operands are written: to the MMA warp.
-    auto hand_over = [&]() {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      tmem_st_wait();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ready);
-    };
 
     for (bool go = any; go;) {
       const int len = unit.len, fresh = unit.fresh, row0 = unit.row0, head = unit.head;
@@ -513,42 +759,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (len > 0) {
-        take_k(n);
-        hand_over();
+        ok = take_k(g, n, wc, ok);
+        hand_over(g);
       }
       group_sync(group);  // the rows' factors and limits
 
       uint64_t nm[ROWS / 2], l[ROWS / 2];  // references (0 for -infinity), negative; sums
 #pragma unroll
       for (int j = 0; j < ROWS / 2; ++j) nm[j] = l[j] = 0;
-      int ref = 0;  // largest value-scale byte so far
+      int ref = 0;  // O's units, see next_units
+      bool far = false;
 
-      for (int t = t0; t < t1 && len > 0; ++t, ++n) {
+      int t = t0;
+      for (; t < t1 && len > 0; ++t, ++n) {
         const int at = t * kTokens + tid;  // this thread's token
         const bool zone = t * kTokens + kTokens - 1 > len - fresh;  // some row may not see all
-        {  // V as f16, over the last one (whose product is complete)
-          const Half h(4 * n + 2 + half);
-          wait(full + 8 * h.slot, h.phase);
-          const uint32_t src = ring + h.slot * kHalfBytes + row_off;
-          if (zone) clean_row(src, x, at, len, fresh, s_nan[group], &s_nans[group]);
-          uint4 v[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) v[u] = lds128(src + ((u ^ x) << 4));
-          if (n > 0) wait(o_done, (n - 1) & 1);
-#pragma unroll
-          for (int u = 0; u < 16; ++u) {  // 8 columns each
-            const uint32_t lo = u & 1 ? v[u >> 1].z : v[u >> 1].x;
-            const uint32_t hi = u & 1 ? v[u >> 1].w : v[u >> 1].y;
-            sts128(v_smem + (u >> 3) * (kTokens * 128) + tid * 128 + (((u & 7) ^ x) << 4),
-                   codes_f16(lo), codes_f16_hi(lo), codes_f16(hi), codes_f16_hi(hi));
-          }
-          // Only now is the slot given back: the loads are known to be done where their
-          // values have been used.  (Given back right after them, with the wait in
-          // between, some of the loads were done after it, when the slot was being
-          // filled again.)
-          __syncwarp();
-          if (lane == 0 && ok) mbar_arrive(empty + 8 * h.slot);
-        }
+        ok = take_v(g, n, zone, at, len, fresh, s_nan[group], &s_nans[group], wc, ok);
         wait(s_done, n & 1);
         tc_fence_after_sync();
         uint32_t s[ROWS];
@@ -556,14 +782,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint8_t* const bytes = s_bytes[group][n % kScaleSlots];
         const float ks = byte_scale(bytes[tid / kKvBlock]);
         const int vb = bytes[8 + tid / kKvBlock];
-        int new_ref = ref;
-        {
-          const uint2 b = *reinterpret_cast<const uint2*>(bytes + 8);
-          const uint32_t b4 = __vmaxu4(b.x, b.y), b2 = __vmaxu4(b4, b4 >> 16);
-          new_ref = max(ref, static_cast<int>(max(b2 & 0xff, b2 >> 8 & 0xff)));
-        }
+        const uint32_t range = s_range[group][n % kScaleSlots];
+        const int lo = range & 0xff, hi = range >> 8;
         tmem_ld_wait();
-        if (t + 1 < t1) take_k(n + 1);
+        if (t + 1 < t1) ok = take_k(g, n + 1, wc, ok);
         // Scores over the references: s c - m, c the factor of a block and row.
         const uint64_t ks2 = pair(ks, ks);
         float top = -INFINITY;
@@ -600,14 +822,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         over();
         const bool first = t == t0;
-        if (group_any(group, first || top > kGrow || new_ref != ref)) {
+        if (group_any(group, first || top > kGrow || !units_hold(ref, lo, hi))) {
           // Each row's largest score, over its reference, in all of the step.
 #pragma unroll
           for (int j = 0; j < ROWS; ++j) {
             const int k = __reduce_max_sync(0xffffffffu, ordered(__uint_as_float(s[j])));
             if (lane == j) s_red[group][quarter][j] = unordered(k);
           }
-          group_sync(group);
+          const int next = next_units(ref, lo, hi);
+          // One word for all: all go through the same barriers, and after a wait that gave
+          // up the threads may differ in what they read.
+          if (group_any(group, next < 0)) {
+            far = true;
+            break;
+          }
           if (tid < ROWS) {
             const float was = s_m[group][tid], zero = was == -INFINITY ? 0.0f : was;
             const float u = zero + fmaxf(fmaxf(s_red[group][0][tid], s_red[group][1][tid]),
@@ -616,8 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             s_m[group][tid] = fmaxf(was, u);
           }
           group_sync(group);
-          const float fr = pow2i(ref - new_ref);
-          ref = new_ref;
+          const float fr = pow2i(ref - next);
+          ref = next;
           uint64_t f[ROWS / 2];
 #pragma unroll
           for (int j = 0; j < ROWS; j += 2) {
@@ -662,7 +890,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             sts16(p_dst + (j + 1) * 128 + ((unit ^ ((j + 1) & 7)) << 4), w16 >> 16);
           }
         }
-        hand_over();
+        hand_over(g);
+      }
+      if (far) {
+        uint32_t sum[ROWS];
+#pragma unroll
+        for (int j = 0; j < ROWS; j += 2) {
+          const float2 v = unpair(l[j / 2]);
+          sum[j] = __float_as_uint(v.x);
+          sum[j + 1] = __float_as_uint(v.y);
+        }
+        tmem_st_x32(mine + kColFarSum, sum);
+        tmem_st_wait();
+        n = far_steps(a, sh, base, t, n, ref);
+        ok = ok && !(n >> 31);
+        n &= 0x7fffffffu;
+        ref = kFarRef;
+        tmem_ld_x32(mine + kColFarSum, sum);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < ROWS; j += 2)
+          l[j / 2] = pair(__uint_as_float(sum[j]), __uint_as_float(sum[j + 1]));
       }
 
       // ---- O / l in the values' own scale: the result, or a part of it
@@ -671,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(o_done, (n - 1) & 1);
         tc_fence_after_sync();
         uint32_t o[ROWS];
-        tmem_ld_x32(mine + kColO, o);
+        tmem_ld_x32(mine + (far ? kColFar : kColO), o);
         tmem_ld_wait();
         tc_fence_before_sync();
 #pragma unroll
@@ -763,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 0) {
     tc_fence_after_sync();
-    tmem_dealloc(s_tmem_base, kGroups * kGroupCols);
+    tmem_dealloc(sh.tmem_base, kGroups * kGroupCols);
   }
 }
 
