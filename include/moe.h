@@ -421,6 +421,9 @@ moe_status_t moe_kv_append(const moe_kv_cache_t* cache, int layer, const moe_bf1
  * below 2^-16 of its row's largest is off by up to 2^-27 of that), whatever the
  * scales of other blocks; values of 2^-100 to 2^110 may stand beside each other.
  * What the pages hold past a sequence's length, and later tokens, take no part.
+ * Where index data does not fit (flagged): keys on a page outside the pool are not
+ * seen, a sequence whose length is negative or past its table sees nothing, rows of
+ * offsets that go down or leave [0, T] are not written.
  * The result does not depend on the other sequences' values or on timing; how
  * a sequence's keys are split (hence rounding) depends on the batch's sizes and
  * lengths and on max_pages.

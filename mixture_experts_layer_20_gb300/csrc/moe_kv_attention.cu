@@ -116,16 +116,24 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// What a step that holds the sequence's end, or new tokens that some rows do not
-// see, needs before its values (32 tokens from position pos on, at v, swizzled)
-// meet the MMAs.  Codes past the end are whatever was in the page: they become
-// zeros.  A NaN among the new tokens concerns only the rows that see its token,
+// A step's block b that lies on a page outside the pool, from its word of Rings.
+constexpr uint32_t kNoBlock = 0x80, kNoBlocks = kNoBlock | kNoBlock << 8;
+__device__ __forceinline__ bool no_page(uint32_t word, int b) {
+  return word >> (8 * b) & kNoBlock;
+}
+
+// What a step that holds the sequence's end, a block without a page (none), or new
+// tokens that some rows do not see, needs before its values (32 tokens from position
+// pos on, at v, swizzled) meet the MMAs.  Codes past the end are whatever was in the
+// page, those without one whatever the ring held: they become zeros.  A NaN among the new tokens concerns only the rows that see its token,
 // but would meet the others' p = 0: it becomes zero too, and nan_from[column]
 // keeps the first position of one, for the end of the unit.  Returns whether
 // there was one.  Called by a warp, a token a lane.
 template <int D>
-__device__ __noinline__ bool clean_values(uint32_t v, int pos, int len, int fresh, int* nan_from) {
+__device__ __noinline__ bool clean_values(uint32_t v, int pos, int len, int fresh, uint32_t none,
+                                          int* nan_from) {
   const int lane = threadIdx.x & 31;
+  const bool no_block = no_page(none, lane >> 4);
   const int at = pos + lane;
   bool found = false;
 #pragma unroll 1
@@ -133,7 +141,7 @@ __device__ __noinline__ bool clean_values(uint32_t v, int pos, int len, int fres
     // the swizzle turns the chunk, and each lane has a row of its own: any order
     const uint32_t addr = v + lane * D + c * 16;
     uint4 w = lds128(addr);
-    if (at >= len) {
+    if (at >= len || no_block) {
       w = make_uint4(0, 0, 0, 0);
     } else if (at > len - fresh) {
       uint32_t words[4] = {w.x, w.y, w.z, w.w};
@@ -168,7 +176,9 @@ template <class S>
 struct Rings {
   static constexpr int kSlots = 2 * kAheadPages;
   uint4 scales[S::kWarps][S::kStages];          // words with the scale bytes: K, K, V, V
-  uint32_t shifts[S::kWarps][S::kStages];       // where in them (bits, a byte each)
+  // where in them (bits, a byte each); the top bit of the first two bytes: the block
+  // lies on a page outside the pool
+  uint32_t shifts[S::kWarps][S::kStages];
   int pages[S::kWarps][kSlots][2];              // of a step's two blocks
   int4 meta[S::kWarps][kSlots];                 // position, head, blocks inside
 };
@@ -241,7 +251,7 @@ __device__ __forceinline__ void load_rings(const KvAttention& a, const CUtensorM
         const int at0 = p0 * 2 * a.cache.heads + d.y, at1 = p1 * 2 * a.cache.heads + d.y;
         row0 = ok0 ? (at0 << ps) + in0 : -1;
         row1 = ok1 && box < kStep ? (at1 << ps) + in1 : -1;
-        uint32_t shifts = 0;
+        uint32_t shifts = (ok0 ? 0u : kNoBlock) | (d.z && !ok1 ? kNoBlock << 8 : 0u);
         const uint32_t dst = smem_u32(&r->scales[mine][stage]);
         auto word = [&](int i, bool ok, const uint8_t* src) {
           src = ok ? src : a.cache.scales;
@@ -500,20 +510,21 @@ __device__ __noinline__ uint32_t far_steps(const KvAttention& a, Shared<S>& sh, 
   for (; t < t1; ++t) {
     const int pos = t * kStep;
     const uint32_t sb = ring + stage * S::kStage;
-    const bool zone = pos + kStep - 1 > q.len - q.fresh;
     ok = __all_sync(0xffffffffu, mbar_wait(k_full + 8 * stage, phase, wc));
     if (!ok) break;
     const uint4 words = sh.rings.scales[warp][stage];
     const uint32_t shifts = sh.rings.shifts[warp][stage];
+    const bool zone = pos + kStep - 1 > q.len - q.fresh || (shifts & kNoBlocks);
     ok = __all_sync(0xffffffffu, mbar_wait(v_full + 8 * stage, phase, wc));
     if (!ok) break;
-    if (zone && clean_values<D>(sb + S::kHalf, pos, q.len, q.fresh, nan_from)) nans = true;
+    if (zone && clean_values<D>(sb + S::kHalf, pos, q.len, q.fresh, shifts, nan_from)) nans = true;
 #pragma unroll 1
     for (int b = 0; b < 2; ++b) {
       const float ks =
-          byte_scale((b ? words.y >> (shifts >> 8 & 0xff) : words.x >> (shifts & 0xff)) & 0xff);
+          byte_scale((b ? words.y >> (shifts >> 8 & 31) : words.x >> (shifts & 31)) & 0xff);
       const float vs =
-          byte_scale((b ? words.w >> (shifts >> 24) : words.z >> (shifts >> 16 & 0xff)) & 0xff);
+          byte_scale((b ? words.w >> (shifts >> 24) : words.z >> (shifts >> 16 & 31)) & 0xff);
+      const bool no_block = no_page(shifts, b);
       uint32_t kw[2][D / 16];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -555,7 +566,8 @@ __device__ __noinline__ uint32_t far_steps(const KvAttention& a, Shared<S>& sh, 
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             s[h] = sc[nt][2 * h + j] * f;
-            if (pos + 16 * b + g + 8 * h > limit[nt * 8 + 2 * t4 + j]) s[h] = -INFINITY;
+            if (no_block || pos + 16 * b + g + 8 * h > limit[nt * 8 + 2 * t4 + j])
+              s[h] = -INFINITY;
           }
           float u = fmaxf(s[0], s[1]);
           u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, 4));
@@ -759,17 +771,19 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       const uint32_t sb = ring + stage * S::kStage;
       ok = __all_sync(0xffffffffu, mbar_wait(k_full + 8 * stage, phase, wc));
       if (!ok) break;
-      const bool zone = pos + kStep - 1 > len - fresh;  // some row may not see all of it
       uint32_t pb[2][NT][2];
+      uint32_t none;  // see no_page
       int kbyte[2], vbyte[2];
       {
         const uint4 words = s_rings.scales[warp][stage];
         const uint32_t shifts = s_rings.shifts[warp][stage];
-        kbyte[0] = words.x >> (shifts & 0xff) & 0xff;
-        kbyte[1] = words.y >> (shifts >> 8 & 0xff) & 0xff;
-        vbyte[0] = words.z >> (shifts >> 16 & 0xff) & 0xff;
+        kbyte[0] = words.x >> (shifts & 31) & 0xff;
+        kbyte[1] = words.y >> (shifts >> 8 & 31) & 0xff;
+        vbyte[0] = words.z >> (shifts >> 16 & 31) & 0xff;
         vbyte[1] = words.w >> (shifts >> 24) & 0xff;
+        none = shifts & kNoBlocks;
       }
+      const bool zone = none || pos + kStep - 1 > len - fresh;  // some row may not see all of it
       // byte 0, as where there is no block, is left out of account
       const int next = next_units(ref, min(vbyte[0] ? vbyte[0] : 255, vbyte[1] ? vbyte[1] : 255),
                                   max(vbyte[0], vbyte[1]));
@@ -822,16 +836,18 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         }
         if (zone) {
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
+          for (int b = 0; b < 2; ++b) {
+            const int at = no_page(none, b) ? INT_MAX - 8 : pos + 16 * b + g;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 // -inf stays -inf with a factor that is not 0
                 f[b][nt][j & 1] = fmaxf(f[b][nt][j & 1], 1.17549435e-38f);
-                if (pos + 16 * b + g + 8 * (j >> 1) > s_limit[warp][nt * 8 + 2 * t4 + (j & 1)])
+                if (at + 8 * (j >> 1) > s_limit[warp][nt * 8 + 2 * t4 + (j & 1)])
                   sc[b][nt][j] = -INFINITY;
               }
+          }
         }
         bool grow = next != ref;
         float top[NT][2];
@@ -883,7 +899,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       }
       ok = __all_sync(0xffffffffu, mbar_wait(v_full + 8 * stage, phase, wc));
       if (!ok) break;
-      if (zone && clean_values<D>(sb + S::kHalf, pos, len, fresh, s_nan[warp])) nans = true;
+      if (zone && clean_values<D>(sb + S::kHalf, pos, len, fresh, none, s_nan[warp])) nans = true;
       {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {

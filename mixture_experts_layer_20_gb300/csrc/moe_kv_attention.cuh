@@ -90,7 +90,8 @@ __device__ __forceinline__ int next_units(int ref, int lo, int hi) {
   return near ? next : -1;
 }
 
-// One sequence, with indexes that do not fit turned into nothing to do.
+// One sequence, with indexes that do not fit turned into nothing to do: offsets
+// into no rows, a length into no keys.
 struct Seq {
   int row0, fresh, len;  // rows of q and their number, keys
 };
@@ -112,7 +113,7 @@ __device__ __forceinline__ Seq read_seq(const KvAttention& a, int s) {
   if (bad_rows || q.len < 0 || q.len > most) {
     atomicOr(a.status, kStatusDeviceCheck);
     if (bad_rows) q.fresh = 0;
-    q.len = static_cast<int>(max(0LL, min(static_cast<long long>(q.len), most)));
+    if (q.len < 0 || q.len > most) q.len = 0;
   }
   return q;
 }

@@ -128,7 +128,8 @@ __device__ __forceinline__ void load_group(const KvAttention& a, const CUtensorM
   struct Step {
     bool there;
     int at, len, head;  // of this lane's block: position; keys of the sequence
-    int page;           // lanes 0 .. 7
+    int page;           // lanes 0 .. 7; -1: past the end, or
+    bool none;          // outside the pool
     int scale;          // lanes 0 .. 7 K's, 8 .. 15 V's
   };
   bool more = true;
@@ -164,6 +165,7 @@ __device__ __forceinline__ void load_group(const KvAttention& a, const CUtensorM
     const bool ok = s.page >= 0 && s.page < a.cache.pages;
     if (in && !ok && lane < 8) atomicOr(a.status, kStatusDeviceCheck);
     if (!in || !ok) s.page = -1;
+    s.none = in && !ok;
     s.scale = 0;
     if (lane < 16 && s.page >= 0)
       s.scale = __ldg(a.cache.scales +
@@ -196,7 +198,8 @@ __device__ __forceinline__ void load_group(const KvAttention& a, const CUtensorM
         const unsigned hi = __reduce_max_sync(0xffffffffu, v);
         const unsigned lo = __reduce_min_sync(0xffffffffu, v ? v : 255u);
         if (lane < 16) scales[step % kScaleSlots][lane] = static_cast<uint8_t>(s0.scale);
-        if (lane == 0) range[step % kScaleSlots] = lo | hi << 8;
+        const unsigned none = __ballot_sync(0xffffffffu, lane < 8 && s0.none);
+        if (lane == 0) range[step % kScaleSlots] = lo | hi << 8 | none << 16;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(full + 8 * h.slot, boxes * box * D);
@@ -213,9 +216,10 @@ __device__ __forceinline__ void load_group(const KvAttention& a, const CUtensorM
     }
 }
 
-// What a step that holds the sequence's end, or new tokens that some rows do not
-// see, needs before a token's values (a row at `src`, its 16-byte units turned
-// by x) meet the MMAs.  Codes past the end are whatever was in the page: they
+// What a step that holds the sequence's end, a block without a page, or new tokens
+// that some rows do not see, needs before a token's values (a row at `src`, its
+// 16-byte units turned by x; `at`: see step_token) meet the MMAs.  Codes past the end
+// are whatever was in the page, those without one whatever the ring held: they
 // become zeros.  A NaN among the new tokens concerns only the rows that see its
 // token, but would meet the others' p = 0: it becomes zero too, and
 // nan_from[column] keeps the first position of one, for the end of the unit.
@@ -379,12 +383,19 @@ struct Shared {
   alignas(16) float f[kGroups][ROWS];       // factors for all threads
   float red[kGroups][4][ROWS];
   alignas(16) uint8_t bytes[kGroups][kScaleSlots][16];
-  uint32_t range[kGroups][kScaleSlots];     // the values' bytes: smallest (but 0), largest
+  // the values' bytes: smallest (but 0), largest; from bit 16 on, blocks on no page of
+  // the pool
+  uint32_t range[kGroups][kScaleSlots];
   int nan[kGroups][D];  // first position of a NaN among the new tokens' values
   int nans[kGroups];
   uint32_t tmem_base;
   int abort;
 };
+
+// Position of a thread's token in step t; past all where its block lies on no page.
+__device__ __forceinline__ int step_token(uint32_t range, int t, int tid) {
+  return range >> (16 + tid / kKvBlock) & 1 ? INT_MAX : t * kTokens + tid;
+}
 
 __device__ __forceinline__ GroupAt group_at(Shared& sh, uint32_t base, int group) {
   const uint32_t ring = base + group * kGroupBytes, full = smem_u32(&sh.bar[group * kBars]);
@@ -458,8 +469,9 @@ __device__ __noinline__ uint32_t far_steps(const KvAttention& a, Shared& sh, uin
     }
   }
   for (bool entry = true; t < t1; ++t, ++n, entry = false) {
-    const int at = t * kTokens + g.tid;
-    const bool zone = t * kTokens + kTokens - 1 > len - fresh;
+    const uint32_t range = sh.range[group][n % kScaleSlots];
+    const int at = step_token(range, t, g.tid);
+    const bool zone = range >> 16 || t * kTokens + kTokens - 1 > len - fresh;
     if (!entry) {
       ok = take_v(g, n, zone, at, len, fresh, sh.nan[group], &sh.nans[group], wc, ok);
       ok = wait_all(g.s_done, n & 1, wc, ok);
@@ -772,8 +784,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       int t = t0;
       for (; t < t1 && len > 0; ++t, ++n) {
-        const int at = t * kTokens + tid;  // this thread's token
-        const bool zone = t * kTokens + kTokens - 1 > len - fresh;  // some row may not see all
+        const uint32_t range = s_range[group][n % kScaleSlots];  // came with the step's K
+        const int at = step_token(range, t, tid);  // this thread's token
+        // some row may not see all
+        const bool zone = range >> 16 || t * kTokens + kTokens - 1 > len - fresh;
         ok = take_v(g, n, zone, at, len, fresh, s_nan[group], &s_nans[group], wc, ok);
         wait(s_done, n & 1);
         tc_fence_after_sync();
@@ -782,8 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint8_t* const bytes = s_bytes[group][n % kScaleSlots];
         const float ks = byte_scale(bytes[tid / kKvBlock]);
         const int vb = bytes[8 + tid / kKvBlock];
-        const uint32_t range = s_range[group][n % kScaleSlots];
-        const int lo = range & 0xff, hi = range >> 8;
+        const int lo = range & 0xff, hi = range >> 8 & 0xff;
         tmem_ld_wait();
         if (t + 1 < t1) ok = take_k(g, n + 1, wc, ok);
         // Scores over the references: s c - m, c the factor of a block and row.
