@@ -71,6 +71,12 @@ __global__ void __launch_bounds__(kAppendWarps * 32) moe_kv_append_kernel(const 
   // Sequence s owns the slots from offsets[s] / 16 + 2 s on: at least as many
   // as the blocks that its new tokens can touch.
   const int slot = blockIdx.x;
+  // Offsets that go down may hide their sequence from the search below: the first
+  // n_seqs slots look at one sequence's each.
+  if (slot < a.n_seqs && head == 0 && lane == 0) {
+    const int from = __ldg(a.offsets + slot), to = __ldg(a.offsets + slot + 1);
+    if (from < 0 || to < from || to > a.T) atomicOr(a.status, kStatusDeviceCheck);
+  }
   const int s = warp_find(a.n_seqs, [&](int i) { return __ldg(a.offsets + i) / kKvBlock + 2 * i <= slot; });
   const int t0 = __ldg(a.offsets + s), t1 = __ldg(a.offsets + s + 1);
   const int len = __ldg(a.kv_lens + s);
