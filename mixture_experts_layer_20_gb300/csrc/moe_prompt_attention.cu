@@ -104,10 +104,16 @@ struct Item {
 
 // Items in order of their key tiles, most first, without a list of them: a
 // sequence's blocks that see exactly L tiles are counted from its length.  A
-// warp, which asks for growing indices.
+// warp, which asks for growing indices.  It looks at 32 sequences at a time, goes on
+// where the last search of the level ended, and passes over spans of sequences that
+// are all too short for the level (each lane knows the longest of one span): with
+// every search from the first sequence on, 4096 prompts of up to 20 tokens (32 heads over
+// 4) took 2941 us instead of 482, with one of 8192 tokens among them 4457 instead of 760.
 struct Order {
   int level, base, count;  // key tiles, index of the level's first item, its items
   int start, len;          // of sequence `lane`
+  int most, span;          // the longest of `span` groups of 32 sequences, from lane x span on
+  int at, before;          // the level's search: group it goes on from, blocks before that
 
   __device__ static void sequence(const PromptParams& p, int s, int& start, int& len) {
     start = len = 0;
@@ -121,44 +127,74 @@ struct Order {
     }
   }
   __device__ static int sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
+  __device__ static int tiles(int len) { return (len + kTile - 1) / kTile; }
   // Blocks of a sequence that see at most `tiles` key tiles.
   __device__ static int blocks(const PromptParams& p, int len, int tiles) {
     const int block = 2 * p.tok;
     return len <= tiles * kTile ? (len + block - 1) / block : tiles * kTile / block;
   }
-  __device__ int at_level(const PromptParams& p) const {
-    int n = blocks(p, len, level) - blocks(p, len, level - 1);
-    for (int s0 = 32; s0 < p.n_seqs; s0 += 32) {
-      int st, l;
-      sequence(p, s0 + (threadIdx.x & 31), st, l);
-      n += blocks(p, l, level) - blocks(p, l, level - 1);
+  __device__ void group(const PromptParams& p, int g, int& st, int& l) const {
+    st = start;
+    l = len;
+    if (g > 0) sequence(p, 32 * g + (threadIdx.x & 31), st, l);
+  }
+  // The first group from g on that may have blocks of this level; past all: none.
+  __device__ int next_group(int g) const {
+    const int lane = g / span;
+    if (lane > 31) return INT_MAX;
+    const unsigned mask =
+        __ballot_sync(0xffffffffu, tiles(most) >= level) & (0xffffffffu << lane);
+    if (mask == 0) return INT_MAX;
+    return max(g, (__ffs(mask) - 1) * span);
+  }
+  __device__ void begin_level(const PromptParams& p) {
+    before = at = 0;
+    int n = 0;
+    if (p.n_seqs <= 32) {
+      n = blocks(p, len, level) - blocks(p, len, level - 1);
+    } else {
+      at = next_group(0);
+      for (int g = at; g <= (p.n_seqs - 1) / 32; g = next_group(g + 1)) {
+        int st, l;
+        group(p, g, st, l);
+        n += blocks(p, l, level) - blocks(p, l, level - 1);
+      }
     }
-    return sum(n) * p.kv_heads;
+    count = sum(n) * p.kv_heads;
   }
   __device__ void init(const PromptParams& p) {
-    sequence(p, threadIdx.x & 31, start, len);
-    int most = len;
-    for (int s0 = 32; s0 < p.n_seqs; s0 += 32) {
-      int st, l;
-      sequence(p, s0 + (threadIdx.x & 31), st, l);
-      most = max(most, l);
+    const int lane = threadIdx.x & 31, groups = (p.n_seqs + 31) / 32;
+    sequence(p, lane, start, len);
+    int top = len;
+    span = 1;
+    most = 0;
+    if (groups > 1) {
+      span = (groups + 31) / 32;
+#pragma unroll 4
+      for (int g = 0; g < groups; ++g) {
+        int st, l;
+        group(p, g, st, l);
+        const int longest = __reduce_max_sync(0xffffffffu, l);
+        if (g / span == lane) most = max(most, longest);
+      }
+      top = most;
     }
-    level = (__reduce_max_sync(0xffffffffu, most) + kTile - 1) / kTile;
-    base = 0;
-    count = level > 0 ? at_level(p) : 0;
+    level = tiles(__reduce_max_sync(0xffffffffu, top));
+    base = count = 0;
+    if (level > 0) begin_level(p);
   }
   // Item i (not below the last one asked for); false: there are not as many.
   __device__ bool get(const PromptParams& p, int i, Item& it) {
     while (level > 0 && i >= base + count) {
       base += count;
-      if (--level > 0) count = at_level(p);
+      if (--level > 0) begin_level(p);
     }
     if (level <= 0) return false;
-    int m = (i - base) / p.kv_heads;
+    const int m = (i - base) / p.kv_heads;
     it.kvh = (i - base) - m * p.kv_heads;
-    for (int s0 = 0;; s0 += 32) {
-      int st = start, l = len;
-      if (s0 > 0) sequence(p, s0 + (threadIdx.x & 31), st, l);
+    for (; at <= (p.n_seqs - 1) / 32; at = next_group(at + 1)) {
+      int st, l;
+      group(p, at, st, l);
       const int below = blocks(p, l, level - 1), n = blocks(p, l, level) - below;
       int c = n;
 #pragma unroll
@@ -166,10 +202,10 @@ struct Order {
         const int u = __shfl_up_sync(0xffffffffu, c, o);
         if (static_cast<int>(threadIdx.x & 31) >= o) c += u;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, c > m);
+      const unsigned hit = __ballot_sync(0xffffffffu, before + c > m);
       if (hit) {
         const int lane = __ffs(hit) - 1;
-        const int block = __shfl_sync(0xffffffffu, below + m - (c - n), lane);
+        const int block = __shfl_sync(0xffffffffu, below + m - before - (c - n), lane);
         it.start = __shfl_sync(0xffffffffu, st, lane);
         it.first = block * 2 * p.tok;
         const int length = __shfl_sync(0xffffffffu, l, lane);
@@ -181,8 +217,9 @@ struct Order {
         }
         return true;
       }
-      m -= __shfl_sync(0xffffffffu, c, 31);
+      before += __shfl_sync(0xffffffffu, c, 31);
     }
+    return false;
   }
 };
 
