@@ -509,6 +509,8 @@ def moe_prompt_attention(q, k, v, seq_offsets, scale=None, out=None, lse=None, w
         raise ValueError("k and v must be [tokens, kv_heads, dim] with the tokens and dim of q")
     vs = _want_rows(v, "v")
     _want(seq_offsets, torch.int32, "seq_offsets")
+    if len(seq_offsets.shape) != 1 or seq_offsets.shape[0] == 0:
+        raise ValueError(f"seq_offsets must be [n_seqs + 1], got {tuple(seq_offsets.shape)}")
     out, lse = _out_lse(q, T, H, out, lse)
     if ws is None:
         ws = _new_status(q.device)
