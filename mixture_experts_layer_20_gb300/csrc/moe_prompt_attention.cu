@@ -438,6 +438,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __all_sync(0xffffffffu, mbar_wait(ifull_bar + 8 * slot, (item_at / kItems) & 1, wc));
     ++item_at;
     Item it = s_item[slot];
+    // A load in flight is not waited for by a later arrive: without the fence the slot
+    // might be written again under it.
+    asm volatile("fence.acq_rel.cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) mbar_arrive(iempty_bar + 8 * slot);
     // the broadcasts tell the compiler that the counts are uniform
