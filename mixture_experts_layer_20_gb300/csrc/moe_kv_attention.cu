@@ -561,7 +561,7 @@ __device__ __noinline__ uint32_t far_steps(const KvAttention& a, Shared<S>& sh, 
         float p[2][2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float f = ks * row_scale[nt][j];
+          const float f = score_factor(ks, row_scale[nt][j]);
           float s[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) f[b][nt][j] = ks * row_scale[nt][j];
+            for (int j = 0; j < 2; ++j) f[b][nt][j] = score_factor(ks, row_scale[nt][j]);
         }
         if (zone) {
 #pragma unroll

@@ -58,6 +58,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 __device__ __forceinline__ float byte_scale(int byte) {
   return __uint_as_float(byte ? static_cast<uint32_t>(byte) << 23 : 0x00400000u);
 }
+// A score's factor from its parts.  Finite: beside an infinite key the other keys of
+// its block are zeros, whose scores are 0 and not 0 x inf.
+__device__ __forceinline__ float score_factor(float key_scale, float row_scale) {
+  return fminf(key_scale * row_scale, 3.402823466e38f);
+}
 // 2^k, 0 below the normal range.
 __device__ __forceinline__ float pow2i(int k) {
   return k < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(min(k, 127) + 127) << 23);

@@ -485,7 +485,7 @@ __device__ __noinline__ uint32_t far_steps(const KvAttention& a, Shared& sh, uin
     if (!entry && t + 1 < t1) ok = take_k(g, n + 1, wc, ok);
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
-      const float y = __uint_as_float(s[j]) * (sh.scale[group][j] * ks);
+      const float y = __uint_as_float(s[j]) * score_factor(ks, sh.scale[group][j]);
       s[j] = at > sh.limit[group][j] ? 0xff800000u : __float_as_uint(y);
       const int top = __reduce_max_sync(0xffffffffu, ordered(__uint_as_float(s[j])));
       if (lane == j) sh.red[group][quarter][j] = unordered(top);
@@ -794,13 +794,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s[ROWS];
         tmem_ld_x32(mine + kColS, s);
         const uint8_t* const bytes = s_bytes[group][n % kScaleSlots];
-        const float ks = byte_scale(bytes[tid / kKvBlock]);
+        const int kb = bytes[tid / kKvBlock];
         const int vb = bytes[8 + tid / kKvBlock];
         const int lo = range & 0xff, hi = range >> 8 & 0xff;
         tmem_ld_wait();
         if (t + 1 < t1) ok = take_k(g, n + 1, wc, ok);
-        // Scores over the references: s c - m, c the factor of a block and row.
-        const uint64_t ks2 = pair(ks, ks);
+        // Scores over the references: s c - m, c the factor of a block and row.  What of the
+        // block's scale is above 2^60 meets the score first: beside an infinite key the
+        // block's other keys are zeros, whose scores are 0 and not 0 x inf.
+        const float low = byte_scale(min(kb, 187)), high = byte_scale(max(kb, 187) - 60);
+        const uint64_t ks2 = pair(low, low), high2 = pair(high, high);
         float top = -INFINITY;
         auto over = [&]() {
           top = -INFINITY;
@@ -808,10 +811,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < ROWS; j += 4) {
             const float4 c = *reinterpret_cast<const float4*>(&s_scale[group][j]);
-            y[j / 2] = fma2(pair(__uint_as_float(s[j]), __uint_as_float(s[j + 1])),
+            y[j / 2] = fma2(mul2(pair(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), high2),
                             mul2(pair(c.x, c.y), ks2), nm[j / 2]);
-            y[j / 2 + 1] = fma2(pair(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])),
-                                mul2(pair(c.z, c.w), ks2), nm[j / 2 + 1]);
+            y[j / 2 + 1] =
+                fma2(mul2(pair(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), high2),
+                     mul2(pair(c.z, c.w), ks2), nm[j / 2 + 1]);
           }
 #pragma unroll
           for (int j = 0; j < ROWS; j += 2) {
