@@ -524,7 +524,7 @@ __device__ __noinline__ uint32_t far_steps(const KvAttention& a, Shared<S>& sh, 
           byte_scale((b ? words.y >> (shifts >> 8 & 31) : words.x >> (shifts & 31)) & 0xff);
       const float vs =
           byte_scale((b ? words.w >> (shifts >> 24) : words.z >> (shifts >> 16 & 31)) & 0xff);
-      const bool no_block = no_page(shifts, b);
+      const int at_g = no_page(shifts, b) ? INT_MAX - 8 : pos + 16 * b + g;
       uint32_t kw[2][D / 16];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -566,8 +566,7 @@ __device__ __noinline__ uint32_t far_steps(const KvAttention& a, Shared<S>& sh, 
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             s[h] = sc[nt][2 * h + j] * f;
-            if (no_block || pos + 16 * b + g + 8 * h > limit[nt * 8 + 2 * t4 + j])
-              s[h] = -INFINITY;
+            if (at_g + 8 * h > limit[nt * 8 + 2 * t4 + j]) s[h] = -INFINITY;
           }
           float u = fmaxf(s[0], s[1]);
           u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, 4));
