@@ -187,3 +187,32 @@ def test_results_repeat(moe, H, K, D, width):
     for _ in range(3):
         two = c.run()
         assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
+
+
+@pytest.mark.parametrize("H", [8, 32, 48])
+def test_a_wait_that_gives_up(moe, H):
+    """With scales far apart and a bound of 1 ns: the call ends, the next one is as before."""
+    n, length, page = 16, 1 << 15, 128
+    g = torch.Generator(device="cuda").manual_seed(H)
+    pages = n * length // page
+    codes = torch.randint(0, 120, (1, pages, 2, 2, page, 128), generator=g, dtype=torch.uint8,
+                          device="cuda")
+    scales = torch.full((1, pages, 2, 2, page // 16), 118, dtype=torch.uint8, device="cuda")
+    scales[:, :, 1] += 12 * torch.randint(0, 2, scales[:, :, 1].shape, generator=g, dtype=torch.uint8,
+                                          device="cuda")
+    cache = moe.KvCache(codes, scales)
+    q = (0.1 * torch.randn((n, H, 128), generator=g, device="cuda")).to(torch.bfloat16)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").view(n, -1)
+    off, lens = (torch.tensor(v, dtype=torch.int32, device="cuda")
+                 for v in (list(range(n + 1)), [length] * n))
+    ws = moe.new_kv_attention_workspace(q, cache, table)
+    ref = moe.moe_kv_attention(q, cache, 0, off, lens, table, ws=ws)
+    assert moe.moe_get_device_status(ws) == moe.MOE_OK
+    try:
+        moe.moe_set_wait_timeout_ns(1)
+        moe.moe_kv_attention(q, cache, 0, off, lens, table, ws=ws)
+        assert moe.moe_get_device_status(ws) == moe.MOE_ERR_TIMEOUT
+    finally:
+        moe.moe_set_wait_timeout_ns(0)
+    again = moe.moe_kv_attention(q, cache, 0, off, lens, table, ws=ws)
+    assert torch.equal(ref[0], again[0]) and torch.equal(ref[1], again[1])
