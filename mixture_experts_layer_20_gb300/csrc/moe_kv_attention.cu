@@ -51,8 +51,15 @@ namespace {
 constexpr int kStep = 32;        // tokens of a warp's step: two blocks
 
 // Steps of a warp, at most, where a CTA has a unit of its own.  Against the even
-// dealing with its second kernel: one sequence, 64 heads over 8, 800 keys 14.3 us
-// for 19.0, 1600 keys (5 steps a warp) 18.4 for 18.9, 2500 keys 22.5 for 19.9.
+// dealing with its second kernel, us with the L2 flushed, one sequence / eight:
+//   8 rows, dim 128   100 keys 12.4 for 17.0 / 11.9 for 18.8, 1920 keys 19.9 for 20.8 / 20.4 for 22.7
+//   16 rows, dim 128  100 keys 12.9 for 16.8 / 12.3 for 20.0, 1600 keys 20.4 for 20.7 / 21.2 for 21.6
+//   8 rows, dim 64    100 keys  9.9 for 16.6 / 11.0 for 16.7, 1920 keys 17.5 for 18.8 / 19.2 for 20.7
+//   16 rows, dim 64   100 keys 10.3 for 15.3 / 11.1 for 17.3, 1600 keys 18.0 for 18.7 / 17.7 for 20.2
+//   32 rows, dim 64   100 keys 12.1 for 17.2 / 12.8 for 19.4, 1120 keys 19.5 for 21.7 / 20.1 for 22.9
+// (the last of each: 5 steps a warp); past it 2500 keys took 22.5 for 19.9 (8 rows,
+// dim 128, one sequence).  The block table's width stands for the lengths, which the
+// host does not know: a table wider than this goes the other way whatever is in it.
 constexpr int kOwnSteps = 5;
 constexpr int kAheadPages = 4;   // steps ahead of the loads that pages are looked up
 

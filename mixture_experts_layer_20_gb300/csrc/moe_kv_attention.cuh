@@ -243,8 +243,8 @@ __device__ __forceinline__ void write_row(const KvAttention& a, int row0, int he
 // lengths alone decide.  A warp takes a row (its lanes four columns each) and,
 // where there are more warps than rows, a share of the parts.  Few units of
 // many parts have their rows split over several CTAs, up to two an SM (6
-// sequences of 131000 keys, 8 heads: 199 us in all instead of 209; four an SM
-// cost 64 shorter sequences 3 us).
+// sequences of up to 131000 keys, 8 heads, L2 flushed before each call: 199 us in all
+// instead of 209; four an SM cost 64 shorter sequences 3 us).
 constexpr int kJoinWarps = 16;
 constexpr int kJoinAt = 4;  // parts that a warp has under way
 template <int D, class Deal>
