@@ -629,6 +629,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int head = it.kvh * p.group + row % p.group;
       const int first_tok = it.first + q * p.tok;
       const int pos = first_tok + my_tok;  // position in the sequence = last key seen
+      // Rows past the sequence's end or the group's (their queries are the next sequence's,
+      // or whatever was there) have no say below.
+      const bool valid = my_tok < (q == 0 ? it.rows_tok[0] : it.rows_tok[1]);
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < n; ++j) {
         ok = __all_sync(0xffffffffu, mbar_wait(sfull_bar + 8 * q, s_phase, wc));
@@ -665,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
         if (j == 0) {
           m = top;
-        } else if (__any_sync(0xffffffffu, top > m + kGrow)) {
+        } else if (__any_sync(0xffffffffu, valid && top > m + kGrow)) {
           // The MMAs before this S, among them the last into O, are complete.
           const float f = top > m ? ex2(m - top) : 1.0f;  // 0 from -inf
           m = fmaxf(m, top);
@@ -707,7 +710,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       o_phase ^= 1u;
       if (ok) {
         tc_fence_after_sync();
-        const bool valid = my_tok < (q == 0 ? it.rows_tok[0] : it.rows_tok[1]);
         const int token = it.start + pos;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         // Each thread has a row; through shared memory (16-byte units turned by

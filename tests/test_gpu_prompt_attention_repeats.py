@@ -27,3 +27,29 @@ def test_the_same_bits(moe, low, high, n, H, K, D):
         again = moe.moe_prompt_attention(q, k, v, off, ws=ws)
         assert torch.equal(again[0], out) and torch.equal(again[1], lse)
     assert moe.moe_get_device_status(ws) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [3, 5, 7, 40, 100, 8, 128])
+def test_each_sequence_by_itself(moe, G, D):
+    """A sequence's bits do not depend on the other sequences, nor on what was computed before: also
+    where a group does not fill its rows of a tile."""
+    lens = [137, 1, 387, 558, 280, 3, 278]
+    g = torch.Generator(device="cuda").manual_seed(G + D)
+    q, k, v = ((2.5 * torch.randn((sum(lens), h, D), generator=g, device="cuda")).to(torch.bfloat16)
+               for h in (G, 1, 1))
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+
+    def run(i, j):
+        a, b = sum(lens[:i]), sum(lens[:j])
+        off = torch.tensor(np.cumsum([0] + lens[i:j]), dtype=torch.int32, device="cuda")
+        return moe.moe_prompt_attention(q[a:b], k[a:b], v[a:b], off, ws=ws)
+
+    out, lse = run(0, len(lens))
+    for _ in range(5):
+        again = run(0, len(lens))
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+    for i, n in enumerate(lens):
+        a = sum(lens[:i])
+        alone = run(i, i + 1)
+        assert torch.equal(alone[0], out[a:a + n]) and torch.equal(alone[1], lse[a:a + n])
