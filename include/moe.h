@@ -371,7 +371,8 @@ moe_status_t moe_graph_destroy(moe_graph_t graph);
  * out [T, heads, dim] bf16 and lse [T, heads] fp32 (or NULL) dense.  Scores,
  * sums and the output are accumulated in fp32; the weights are rounded to
  * bf16 for the tensor cores.  Later tokens take no part, whatever they hold
- * (NaN and infinities too).  ws: at least 256 bytes (the status word and the
+ * (NaN and infinities too); a sequence's results do not depend on the others or on
+ * timing.  ws: at least 256 bytes (the status word and the
  * counter that hands out the work, left at zero by every call). */
 moe_status_t moe_prompt_attention(const moe_bf16* q, const moe_bf16* k, const moe_bf16* v,
                                   long long q_stride, long long k_stride, long long v_stride,

@@ -77,3 +77,21 @@ def test_offsets_that_do_not_fit(moe, T, off):
                       _i32(4 + _table(n, 16)), ws=ws)
     assert moe.moe_get_device_status(ws) == moe.MOE_ERR_DEVICE_CHECK
     assert cache.codes[0, :4].eq(0).all() and cache.codes[0, 16 * n + 4:].eq(0).all()
+
+
+@pytest.mark.parametrize("new", [1, 5])
+def test_the_last_positions_there_are(moe, new):
+    """A table of 2^31 positions (pages shared by many entries), written at its end."""
+    last = (1 << 31) - 1
+    g = torch.Generator().manual_seed(9)
+    k, v = _rows((new, 1, 64), g), _rows((new, 1, 64), g)
+    cache = moe.new_kv_cache(3, 1, 128, 64)
+    table = torch.full((1, 1 << 24), 1, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    moe.moe_kv_append(cache, 0, k.cuda(), v.cuda(), _i32([0, new]), _i32([last]), table, ws=ws)
+    assert moe.moe_get_device_status(ws) == moe.MOE_OK
+    codes = np.zeros((3, 2, 1, 128, 64), np.uint8)
+    scales = np.zeros((3, 2, 1, 8), np.uint8)
+    R.append(codes, scales, k.double().numpy(), v.double().numpy(), [0, new], [127], np.array([[1]]))
+    assert np.array_equal(cache.codes[0].cpu().numpy(), codes)
+    assert np.array_equal(cache.scales[0].cpu().numpy(), scales)
