@@ -88,9 +88,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32) moe_kv_append_kernel(const 
   }
   const int first = len - fresh;  // position of the first new token
   const int block = first / kKvBlock + (slot - (t0 / kKvBlock + 2 * s));
+  // (positions go up to 2^31 - 1: none past the last block is computed)
+  if (slot < t0 / kKvBlock + 2 * s || fresh == 0 || block > (len - 1) / kKvBlock) return;
   const int begin = max(first, block * kKvBlock);
-  const int end = block * kKvBlock + min(len - block * kKvBlock, kKvBlock);  // below 2^31
-  if (slot < t0 / kKvBlock + 2 * s || begin >= end) return;
+  const int end = block * kKvBlock + min(len - block * kKvBlock, kKvBlock);
   const int page = __ldg(a.block_table + static_cast<size_t>(s) * a.max_pages +
                          block * kKvBlock / a.cache.page);
 
